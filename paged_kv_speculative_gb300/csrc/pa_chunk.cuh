@@ -23,14 +23,15 @@
 // more than 8 (2^8 in P), so O is rescaled rarely, and the two threads of a row need only a vote per tile (they meet in shared
 // memory when one of them wants M raised); O / l is the same whatever M was. Sums stay fp32; P is rounded to bf16 (the output's
 // type; l sums the unrounded values).
-// FP8. The tiles are widened to f16 on their way into the ring, once for all rows of the unit, by the softmax warps in the time
+// FP8. The tiles are widened to 16 bits on their way into the ring, once for all rows of the unit, by the softmax warps in the time
 // they wait for their next scores: one page of K or V a warp and tile, read from global memory (which warp 0, a few tiles
-// ahead, brings into L2), codes times scale, written in the layout of the bf16 tiles; Q becomes f16 after a power-of-two scale
-// of its row (exactly: bf16 has 8 significant bits) and P is rounded to f16, so everything behind is the bf16 path. f16 has 11
-// bits (an entry is off by 2^-11 of itself at most, where E4M3 left 2^-4) but not the range of the scales: a K tile is scaled
-// by 2^(4 - e), 2^e just above its largest scale, which its scores are multiplied back by; V by an exponent that a unit carries
-// from tile to tile and raises when a tile's largest scale passes it by 2^3 or more, with O rescaled as for M (448 times a scale
-// below 2^7 still is an f16; steps are at most 2^-27 of the largest scale).
+// ahead, brings into L2), codes times scale, written in the layout of the bf16 tiles; everything behind is the bf16 path. K and Q are
+// f16: 11 bits (a key's entry is off by 2^-11 of itself at most, where E4M3 left 2^-4), so a K tile is scaled by 2^(4 - e), 2^e just
+// above its largest scale, which its scores are multiplied back by, and a row of Q by a power of two.
+// P and V are bf16, as there: P has to reach as far down as l does. In f16 a weight below 2^-25 of the reference is 0, and behind one
+// key that stands 17.4 nats above the others their whole part of the output goes (the cost: single tokens 159.5 to 167 us,
+// 512 tokens over 16384, 8/1 heads of 256, 110 to 114, 1024 over 8192 170.5 either way). V counts in 2^30, so that scales of
+// up to 1e30 sum in fp32 and those down to 2^-87 keep every code.
 // Measured for 1024 tokens over 8192, 32/4 heads of 128: in 8 bits throughout with P in two E4M3 terms 297 us (scales at every
 // score are 160 16-byte shared loads a warp and tile); with V alone widened by two warps of their own 204 us; with six warps of
 // their own for both 181 to 185, and 113 to 123 for 512 tokens over 16384, 8/1 heads of 256; this way 177 and 114. bf16: 121.
@@ -174,12 +175,11 @@ struct ChunkCfg {
 struct __align__(16) ChunkTile {
   int page[8];        // page x KV heads + head; -1: none (zeros)
   int keys;           // tokens of the tile that exist; -1: there is no such tile
-  float up[2];        // 2^(4 - e) of K and of V
-  float k_factor;     // 2^(e - 4) of K: what its scores count in
-  float o_factor;     // of O, when V's exponent has risen
-  float unit;         // 2^(e - 4) of V: what O counts in
-  int pad[2];
+  float k_up;         // 2^(4 - e) of K
+  float k_factor;     // 2^(e - 4): what its scores count in
+  int pad[5];
 };
+constexpr float kChunkVUnit = 1073741824.f;  // FP8: what V, and with it O, counts in (2^30)
 
 // Line length of a unit: its visible keys plus this many tokens for its start and end (three tiles; 32 ragged sequences 73.9 us,
 // with two or four 75.7; 64 prompts of 300 tokens 139 and 144).
@@ -503,18 +503,12 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
               const int pg = __ldg(row + t * C::kPages + lane);
               return static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages) ? pg : -2;
             };
-            struct Scales {
-              float4 k, v;
-            };
-            auto scales = [&](int t, int pg) {  // this lane's four tokens; what lies behind E is read as 0
-              Scales x{};
+            auto scales = [&](int t, int pg) {  // K's, of this lane's four tokens; what lies behind E is read as 0
               const int id = __shfl_sync(0xffffffffu, pg, lane / 4);
               const int left = E - t * C::kTok - 4 * lane;
-              if (lane >= C::kTok / 4 || t >= t1 || left <= 0 || id < 0) return x;
+              if (lane >= C::kTok / 4 || t >= t1 || left <= 0 || id < 0) return make_float4(0.f, 0.f, 0.f, 0.f);
               const size_t at = (static_cast<size_t>(id) * p.num_kv_heads + w.at.g) * kPage + (4 * lane) % kPage;
-              x.k = *reinterpret_cast<const float4*>(p.k_scale + at);
-              x.v = *reinterpret_cast<const float4*>(p.v_scale + at);
-              return x;
+              return *reinterpret_cast<const float4*>(p.k_scale + at);
             };
             auto largest = [&](int t, const float4& x) {
               const int left = E - t * C::kTok - 4 * lane;
@@ -524,14 +518,16 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
               return chunk_warp_max(left > 3 ? fmaxf(m, fabsf(x.w)) : m);
             };
             auto exponent = [](float top) { return top > 1e-30f ? ilogbf(fminf(top, 1e30f)) + 1 : -98; };  // top < 2^e
-            int t = w.at.t, ev = 0;
+            int t = w.at.t;
             int pg = page_id(t), pg1 = page_id(t + 1);
-            Scales sc = scales(t, pg);
+            float4 sc = scales(t, pg);
             for (; t < t1; ++t, ++n) {
               const int pg2 = page_id(t + 2);
-              const Scales sc1 = scales(t + 1, pg1);
-              // the page's codes into L2: lanes 0 .. 7 K, 16 .. 23 V
+              const float4 sc1 = scales(t + 1, pg1);
+              // the page's codes into L2: lanes 0 .. 7 K, 16 .. 23 V; V's scales: lanes 8 .. 15
               const int far = __shfl_sync(0xffffffffu, pg, lane & 7);
+              if (lane >= 8 && lane < 8 + C::kPages && far >= 0)
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.v_scale + (static_cast<size_t>(far) * p.num_kv_heads + w.at.g) * kPage));
               if ((lane & 15) < C::kPages && far >= 0)
                 asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(
                                  static_cast<const uint8_t*>(lane < 16 ? p.k_cache : p.v_cache) +
@@ -541,18 +537,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
               if (pg == -2) atomicOr(err, kErrPageRange);
               ChunkTile x;
               x.keys = min(C::kTok, E - t * C::kTok);
-              const int ek = exponent(largest(t, sc.k));
-              const int te = exponent(largest(t, sc.v));
-              x.o_factor = 1.f;
-              if (t == w.at.t) ev = te;
-              else if (te > ev + 3) {
-                x.o_factor = exp2f(static_cast<float>(ev - te));
-                ev = te;
-              }
-              x.up[0] = exp2f(static_cast<float>(4 - ek));
-              x.up[1] = exp2f(static_cast<float>(4 - ev));
+              const int ek = exponent(largest(t, sc));
+              x.k_up = exp2f(static_cast<float>(4 - ek));
               x.k_factor = exp2f(static_cast<float>(ek - 4));
-              x.unit = exp2f(static_cast<float>(ev - 4));
               if (!(ok = put(x, pg < 0 ? -1 : pg * p.num_kv_heads + w.at.g, n % C::kTileSlots))) break;
               pg = pg1;
               pg1 = pg2;
@@ -632,7 +619,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
       auto all_wait = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
       constexpr uint32_t fmt = FP8 ? tc::kF16 : tc::kBF16;
       constexpr uint32_t idS = tc::idesc(fmt, fmt, tc::kKMajor, tc::kKMajor, 128, C::kTok);
-      constexpr uint32_t idPV = tc::idesc(fmt, fmt, tc::kKMajor, tc::kMNMajor, 128, D);
+      constexpr uint32_t idPV = tc::idesc(tc::kBF16, tc::kBF16, tc::kKMajor, tc::kMNMajor, 128, D);
       const uint32_t aKV = smem_addr(sKV), aQ = smem_addr(sQ);
       int n = 0;              // tiles so far: K at ring entry 2 n, V at 2 n + 1
       int ns[2] = {0, 0};     // S products issued for each row tile
@@ -753,7 +740,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
       const ChunkTile& x = tiles[m % 8];
       j.page = x.page[job];
       j.keys = x.keys;
-      j.up = x.up[widens_v];
+      j.up = widens_v ? 1.f / kChunkVUnit : x.k_up;
       more_tiles = ok && j.keys >= 0;
     };
     auto fetch = [&](const Job& j, uint4 (&code)[kLoads], float (&f)[kLoads]) {
@@ -783,15 +770,18 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const float fs = f[k] * j.up;
-        const uint32_t hi = pack_f16(fs, fs);
         const uint32_t u[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(u[i], o[2 * i], o[2 * i + 1]);
         if (widens_v) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = mul_f16x2(o[i], hi);
+          for (int i = 0; i < 8; ++i) {
+            const float2 v = __fmul2_rn(f16x2_to_f32x2(o[i]), make_float2(fs, fs));
+            o[i] = pack_bf16(v.x, v.y);
+          }
         } else {
+          const uint32_t hi = pack_f16(fs, fs);
           // K: the scale as two f16 terms (one would put the same 2^-11 on all of a key's products, and so on its score): code x low,
           // then one rounding of code x high + that
           const float rest = fs - f16x2_to_f32x2(hi).x;
@@ -895,7 +885,6 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
         if (lane == 0) mbar_arrive_one(smem_addr(&qfull[s]));
       }
       float M = -INFINITY, l = 0.f;
-      float unit = 1.f;  // what O's entries count in (FP8: 2^(e - 4))
       for (int t = t0; t < t1; ++t, ++n, ++i_s) {
         const int buf = NS == 1 ? 0 : i_s & 1;
         const uint32_t tSb = tS(s, buf) + lanes;
@@ -905,12 +894,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C::kCols; c += 32) tmem_ld32(tSb + h * C::kCols + c, x + c);
         tc::wait_ld();
-        float cr_t = cr, factor = 1.f;  // FP8: the tile's scores count in k_factor; O's factor when V's exponent has risen
+        float cr_t = cr;  // FP8: the tile's scores count in k_factor
         if constexpr (FP8) {
-          const ChunkTile& x = tiles[n % 8];  // this warp has seen its barrier when it peeked at the tile
-          cr_t = cr * x.k_factor;
-          factor = x.o_factor;
-          unit = x.unit;
+          cr_t = cr * tiles[n % 8].k_factor;  // this warp has seen its barrier when it peeked at the tile
           __syncwarp();
           if (lane == 0) mbar_arrive_one(smem_addr(&tempty[n % 8]));
         }
@@ -926,14 +912,13 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
           m4[(c >> 1) & 3] = fmaxf(fmaxf(m4[(c >> 1) & 3], __uint_as_float(x[c])), __uint_as_float(x[c + 1]));
         float mx = cr_t * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // both halves' scores are in registers once both warps have voted: P may then overwrite S
-        if (named_or(pair, 64, mx > M + 8.f || (FP8 && factor != 1.f))) {
+        if (named_or(pair, 64, mx > M + 8.f)) {
           ex_max[h * 128 + r] = mx;
           named_sync(pair, 64);
           mx = fmaxf(ex_max[r], ex_max[128 + r]);
           const bool up = mx > M + 8.f;
-          float f = up ? fast_exp2(M - mx) : 1.f;  // 0 on the row's first tile
+          const float f = up ? fast_exp2(M - mx) : 1.f;  // 0 on the row's first tile
           l *= f;
-          f *= factor;
           M = up ? mx : M;
           if (t > t0) {
             pv_done(i_s - 1);
@@ -963,7 +948,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
             const float2 d = __ffma2_rn(make_float2(__uint_as_float(x[c0 + c]), __uint_as_float(x[c0 + c + 1])), cr2, sh2);
             const float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
             l2[(c >> 1) & 1] = __fadd2_rn(l2[(c >> 1) & 1], e);
-            pw[c / 2] = FP8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+            pw[c / 2] = pack_bf16(e.x, e.y);
           }
           tc::st16(tSb + (h * C::kCols + c0) / 2, pw);
         }
@@ -1005,7 +990,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
       pv_done(i_s - 1);
       tc::fence_after_sync();
       const bool whole = t0 == 0 && t1 == w.tiles();
-      const float inv = whole || l != 0.f ? unit / l : 0.f;  // a part may hold no key that the row sees
+      const float inv = whole || l != 0.f ? (FP8 ? kChunkVUnit : 1.f) / l : 0.f;  // a part may hold no key that the row sees
       if (whole) {
         uint16_t* dst = p.out + (static_cast<int64_t>(w.tok0() + s * TQ + tok) * p.num_q_heads + w.at.g * G + head) * D;
 #pragma unroll 1
