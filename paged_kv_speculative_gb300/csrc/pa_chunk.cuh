@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
   uint64_t* drain = odone + 2;
   uint32_t* tbase = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
+  volatile int* progress = reinterpret_cast<volatile int*>(tbase + 2);  // bf16: ring entries of V that have been filled
   ChunkPos* s_pos = reinterpret_cast<ChunkPos*>(tbase + 4);  // [2]
   ChunkSeq* s_seq = reinterpret_cast<ChunkSeq*>(s_pos + 2);  // [2]: the cuts' sequences
   struct WalkState {
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
     mbar_init(smem_addr(qfree), 1);
     mbar_init(smem_addr(drain), 1);
     *abort_flag = 0;
+    *progress = 0;
     fence_mbar_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
@@ -466,6 +468,17 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
     *abort_flag = 1;
     atomicOr(err, kErrTimeout);
     return false;
+  };
+  // Two waits of the bf16 path may span a whole unit, whose keys can take many times the limit: for its query rows' place, and by the
+  // softmax of row tile 1 behind a unit that has none. They run out when the limit passes without a new tile. (The other waits span a
+  // tile or two; all of them in this form took 3 to 8 % more time.)
+  auto wait_unit = [&](uint64_t* bar, int phase) {
+    for (int seen = -1;;) {
+      if (mbar_wait_bounded(smem_addr(bar), static_cast<uint32_t>(phase) & 1u)) return true;
+      const int now = *progress;
+      if (now == seen || *abort_flag) return wait(bar, phase);
+      seen = now;
+    }
   };
   uint8_t* sKV = sm + C::kOffKV;
   uint8_t* sQ = sm + C::kOffQ;
@@ -575,6 +588,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
             if (lane == 0) {
               if (e >= C::kSlots) good = !*abort_flag && wait(&kvempty[slot], e / C::kSlots - 1);
               if (good) mbar_arrive_expect_tx(smem_addr(&kvfull[slot]), pages * (kPage * C::kRowB));
+              if (is_v) *progress = e;
             }
             if (!__shfl_sync(0xffffffffu, good, 0)) {
               ok = false;
@@ -600,7 +614,7 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
         int u = 0;
         uint32_t qphase[2] = {0, 0};
         for (; !w.done(); w.next(), ++u) {
-          if (u > 0 && (*abort_flag || !wait(qfree, u - 1))) break;
+          if (u > 0 && (*abort_flag || !wait_unit(qfree, u - 1))) break;
           for (int s = 0; s < NT; ++s) {
             if (s * TQ >= w.ntok()) break;
             const uint32_t bar = smem_addr(&qfull[s]);
@@ -883,6 +897,9 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive_one(smem_addr(&qfull[s]));
+      }
+      if constexpr (!FP8 && NT == 2) {
+        if (s == 1) ok = __all_sync(0xffffffffu, ok && wait_unit(&sfull[1], i_s)) != 0;
       }
       float M = -INFINITY, l = 0.f;
       for (int t = t0; t < t1; ++t, ++n, ++i_s) {
