@@ -55,8 +55,10 @@ struct Caches {
 bool caches(PyObject* k_, PyObject* v_, PyObject* ks_, PyObject* vs_, int dev, bool fp8, int64_t hkv, int64_t d, Caches* c) {
   const at::Tensor *k = tensor(k_), *v = tensor(v_);
   if (!k || !v || k->dim() != 4 || v->sizes() != k->sizes()) return false;
-  const size_t size = fp8 ? 1 : 2;
-  if (k->size(1) != hkv || k->size(2) != 16 || k->size(3) != d || k->element_size() != size || v->element_size() != size) return false;
+  auto typed = [&](const at::Tensor& t) {
+    return fp8 ? t.scalar_type() == at::kByte || t.scalar_type() == at::kFloat8_e4m3fn : t.scalar_type() == at::kBFloat16;
+  };
+  if (k->size(1) != hkv || k->size(2) != 16 || k->size(3) != d || !typed(*k) || !typed(*v)) return false;
   if (!on(*k, dev) || !on(*v, dev) || !k->is_contiguous() || !v->is_contiguous()) return false;
   *c = Caches{k->data_ptr(), v->data_ptr(), nullptr, nullptr, k->size(0)};
   if (!fp8) return true;

@@ -418,6 +418,7 @@ def greedy_verdict(logits: torch.Tensor, input_ids: torch.Tensor, query_lens: to
 # These calls take few microseconds on the device, so their checks are written as one expression of plain attribute reads
 # each (about 0.1 us a read); what failed is found out afterwards, by _explain.
 _BF16, _F32, _F64, _I32, _I64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
+_FP8_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
@@ -503,11 +504,12 @@ def _rows(t: torch.Tensor, name: str) -> int:
 
 def _caches_ok(dev: int, k_cache, v_cache, k_scale, v_scale, kv_dtype: int, num_kv_heads: int, head_dim: int,
                num_pages: Optional[int] = None):
-    """Checks a layer's caches [num_pages, Hkv, 16, D] and, for FP8, their scales [num_pages, Hkv, 16]."""
-    size = 1 if kv_dtype == KV_FP8_E4M3 else 2
+    """Checks a layer's caches [num_pages, Hkv, 16, D], bf16 or E4M3 codes (float8_e4m3fn or uint8), and, for FP8, their scales
+    [num_pages, Hkv, 16]."""
+    types = _FP8_TYPES if kv_dtype == KV_FP8_E4M3 else (_BF16,)
     shape = k_cache.shape
     if (shape[1:] == (num_kv_heads, 16, head_dim) and (num_pages is None or shape[0] == num_pages) and v_cache.shape == shape
-            and k_cache.element_size() == size and v_cache.element_size() == size and k_cache.is_contiguous()
+            and k_cache.dtype in types and v_cache.dtype in types and k_cache.is_contiguous()
             and v_cache.is_contiguous() and k_cache.get_device() == dev and v_cache.get_device() == dev):
         if kv_dtype != KV_FP8_E4M3:
             return
@@ -518,8 +520,9 @@ def _caches_ok(dev: int, k_cache, v_cache, k_scale, v_scale, kv_dtype: int, num_
             return
         _explain(dev, k_scale=(k_scale, _F32, (shape[0], num_kv_heads, 16)), v_scale=(v_scale, _F32, (shape[0], num_kv_heads, 16)))
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dim() == 4 and t.element_size() != size:
-            raise ValueError(f"{name} has elements of {t.element_size()} bytes, expected {size}")
+        if t.dtype not in types:
+            raise ValueError(f"{name} must be {' or '.join(map(str, types))}, got {t.dtype}")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, name)
         pages = num_pages if num_pages is not None else k_cache.shape[0]
         if t.get_device() != dev or tuple(t.shape) != (pages, num_kv_heads, 16, head_dim):
@@ -640,7 +643,7 @@ class PagePool:
 
     The block table [B, stride], the lengths [B] and the reference counts [num_pages] (int32 device tensors) are the
     caller's and travel with each call. ``k_caches`` / ``v_caches``: one [num_pages, Hkv, 16, D] tensor a layer, bf16,
-    or 8-bit with ``k_scales`` / ``v_scales`` [num_pages, Hkv, 16]."""
+    or E4M3 codes (as float8_e4m3fn or uint8) with ``k_scales`` / ``v_scales`` [num_pages, Hkv, 16]."""
 
     def __init__(self, k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor],
                  k_scales: Optional[Sequence[torch.Tensor]] = None, v_scales: Optional[Sequence[torch.Tensor]] = None):

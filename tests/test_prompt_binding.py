@@ -1,0 +1,104 @@
+"""The prompt-side calls of the binding, which has two ways into the C ABI: the module pa_fast and Python."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_speculative_gb300 import _build, pa_verify as pv
+
+PAGE = 16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+
+
+@pytest.fixture(params=["native", "python"])
+def way(request, monkeypatch):
+    """Through pa_fast, which has to be there, or without it."""
+    if request.param == "python":
+        monkeypatch.setattr(pv, "_fast_module", False)
+    else:
+        assert pv._fast()
+    return request.param
+
+
+def setup(kv, pages=12, hkv=2, d=128, seed=0):
+    """One layer's caches and one call's arguments, on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t, hq, i32 = 20, 4, dict(dtype=torch.int32, device="cuda")
+    shape = (pages, hkv, PAGE, d)
+    s = dict(kv=kv)
+    for which in "kv":
+        x = torch.randn(shape, device="cuda", generator=g)
+        if kv == pv.KV_BF16:
+            s[which + "c"], s[which + "s"] = x.to(torch.bfloat16), None
+        else:
+            s[which + "s"] = (x.abs().amax(-1) / 448).contiguous()
+            s[which + "c"] = (x / s[which + "s"][..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    rows = lambda h: torch.randn((t, h, d), device="cuda", generator=g).to(torch.bfloat16)
+    s["q"], s["k"], s["v"] = rows(hq), rows(hkv), rows(hkv)
+    s["positions"] = torch.randint(-999, 999, (2, t), device="cuda", generator=g).to(torch.int32)
+    s["inv_freq"] = 1e4 ** (-torch.arange(d // 2, dtype=torch.float64, device="cuda") / (d // 2))
+    s["pair_axis"] = torch.arange(d // 2, **i32) % 2
+    s["slots"] = torch.randperm(pages * PAGE, device="cuda", generator=g)[:t]
+    s["table"] = torch.tensor([[5, 0, 11, -1], [2, 7, -1, -1]], **i32)
+    s["ctx"], s["ql"] = torch.tensor([40, 19], **i32), torch.tensor([13, 7], **i32)
+    s["ref"] = torch.zeros(pages, **i32)
+    s["ref"][torch.tensor([5, 0, 11, 2, 7], device="cuda")] = 1
+    return s
+
+
+ROPE = ("q", "k", "v", "positions", "inv_freq", "pair_axis", "slots", "kc", "vc", "ks", "vs")
+CHUNK = ("q", "kc", "vc", "ks", "vs", "table", "ctx", "ql")
+
+
+def rope(s, **kw):
+    return pv.rope_write(*[s[n] for n in ROPE], s["kv"], **kw)
+
+
+def chunk(s, **kw):
+    return pv.ChunkAttention(4, 2, 128, s["kv"], 12, 4, max_seqs=2)(*[s[n] for n in CHUNK], 1 / math.sqrt(128), **kw)
+
+
+# ------------------------------------------------------------------ cache types
+def test_cache_types_on_the_host():
+    """Python's check, on host tensors (device -1)."""
+    shape = (3, 2, 16, 64)
+    of = lambda t: torch.zeros(shape, dtype=torch.uint8 if t.itemsize == 1 else torch.int16).view(t)
+    scale = torch.ones(shape[:3])
+    ok = lambda k, v, kv: pv._caches_ok(-1, of(k), of(v), scale, scale, kv, 2, 64)
+    ok(torch.bfloat16, torch.bfloat16, pv.KV_BF16)
+    ok(torch.uint8, torch.float8_e4m3fn, pv.KV_FP8_E4M3)
+    for bad, good, kv in [(t, torch.bfloat16, pv.KV_BF16) for t in (torch.float16, torch.int16, torch.uint8)] + [
+            (t, torch.uint8, pv.KV_FP8_E4M3) for t in (torch.float8_e5m2, torch.int8, torch.bfloat16)]:
+        for k, v in ((bad, good), (good, bad)):
+            with pytest.raises(ValueError, match="must be torch"):
+                ok(k, v, kv)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv,other", [(pv.KV_BF16, torch.float16), (pv.KV_BF16, torch.int16), (pv.KV_FP8_E4M3, torch.float8_e5m2),
+                                      (pv.KV_FP8_E4M3, torch.int8)])
+def test_caches_of_another_type_of_the_same_size_are_refused(way, kv, other):
+    s = setup(kv)
+    for name in ("kc", "vc"):
+        bad = {**s, name: s[name].view(other)}
+        before = bad[name].clone()
+        for call in (rope, chunk):
+            with pytest.raises(ValueError, match="must be torch"):
+                call(bad)
+        with pytest.raises(ValueError, match="must be torch"):
+            pv.PagePool([bad["kc"]], [bad["vc"]], None if s["ks"] is None else [s["ks"]], None if s["vs"] is None else [s["vs"]])
+        assert torch.equal(bad[name].view(torch.uint8), before.view(torch.uint8))
+
+
+@pytest.mark.gpu
+def test_codes_as_float8_and_as_bytes(way):
+    s = setup(pv.KV_FP8_E4M3)
+    want = chunk(s)
+    f8 = {**s, "kc": s["kc"].view(torch.float8_e4m3fn), "vc": s["vc"].view(torch.float8_e4m3fn)}
+    assert torch.equal(chunk(f8), want)
+    rope(f8)  # writes into s's caches
+    pv.PagePool([f8["kc"]], [f8["vc"]], [s["ks"]], [s["vs"]])
