@@ -470,6 +470,15 @@ def _empty(shape, dtype, device: torch.device, stream: Optional[torch.cuda.Strea
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeroed(n: int, dtype, device: torch.device) -> torch.Tensor:
+    """Zeros that a call on any stream finds as zeros: the current stream, which fills them, is waited for."""
+    with torch.cuda.device(device):
+        t = torch.zeros(n, dtype=dtype, device=device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return t
+
+
 def _explain(dev: int, **wanted):
     """Raises for the first of ``name=(tensor, dtype, shape)`` that is not contiguous, of that type and shape (None: any) on
     device ``dev``."""
@@ -577,7 +586,8 @@ def rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
 
 
 class ChunkAttention:
-    """pa_chunk_attention for batches of up to ``max_seqs`` sequences, with a zero-initialised device workspace."""
+    """pa_chunk_attention for batches of up to ``max_seqs`` sequences, with a zero-initialised device workspace (the object has
+    to live until its calls have run; making one waits for the current stream)."""
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, kv_dtype: int, num_pages: int,
                  block_table_stride: int, max_seqs: int = 1024, device: Optional[torch.device] = None):
@@ -591,7 +601,7 @@ class ChunkAttention:
         need = lib().pa_chunk_workspace_bytes(ctypes.byref(self._desc(max_seqs, 0, 0)))
         if need == 0:
             raise PaVerifyError(ERR_UNSUPPORTED, last_error())
-        self.workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        self.workspace = _zeroed(need, torch.uint8, self.device)
         self._plain = (num_q_heads, num_kv_heads, head_dim, kv_dtype, num_pages, block_table_stride, max_seqs, self.sm_count,
                        self.workspace.data_ptr(), need, self.device.index)
 
@@ -643,7 +653,8 @@ class PagePool:
 
     The block table [B, stride], the lengths [B] and the reference counts [num_pages] (int32 device tensors) are the
     caller's and travel with each call. ``k_caches`` / ``v_caches``: one [num_pages, Hkv, 16, D] tensor a layer, bf16,
-    or E4M3 codes (as float8_e4m3fn or uint8) with ``k_scales`` / ``v_scales`` [num_pages, Hkv, 16]."""
+    or E4M3 codes (as float8_e4m3fn or uint8) with ``k_scales`` / ``v_scales`` [num_pages, Hkv, 16]. The pool has to live until
+    its calls have run; making one waits for the current stream."""
 
     def __init__(self, k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor],
                  k_scales: Optional[Sequence[torch.Tensor]] = None, v_scales: Optional[Sequence[torch.Tensor]] = None):
@@ -667,8 +678,8 @@ class PagePool:
         need = lib().pa_pages_workspace_bytes(ctypes.byref(PagesDesc(0, 1, self.num_pages)))
         if need == 0:
             raise PaVerifyError(ERR_UNSUPPORTED, last_error())
-        self.workspace = torch.zeros(need, dtype=torch.uint8, device=self.device)
         self.errors = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.workspace = _zeroed(need, torch.uint8, self.device)
         self._scratch = (self.errors.data_ptr(), self.workspace.data_ptr(), need)
         self._pool = _fast().pool_new(self.num_pages, hkv, d, self.kv_dtype, self.dev, *self._scratch,
                                       *[[t.data_ptr() for t in g] for g in self.caches]) if _fast() else None

@@ -102,3 +102,27 @@ def test_codes_as_float8_and_as_bytes(way):
     assert torch.equal(chunk(f8), want)
     rope(f8)  # writes into s's caches
     pv.PagePool([f8["kc"]], [f8["vc"]], [s["ks"]], [s["vs"]])
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.gpu
+def test_a_new_object_on_another_stream(way):
+    """A pool and a chunk attention made while their own stream is busy, on memory that held ones, and used on another stream at
+    once: their workspaces have to be zeros there (a ticket that is not leaves the growing rows unserved)."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    s, n = setup(pv.KV_BF16), 4
+    table, lens, ref = torch.zeros((n, 5000), **i32), torch.zeros(n, **i32), torch.zeros(12, **i32)
+    new = torch.tensor([20, 3, 0, 33], **i32)
+    need = pv.PagePool([s["kc"]], [s["vc"]]).workspace.numel()
+    chunk(s)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dirty = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    del dirty
+    torch.cuda._sleep(200_000_000)  # clocks: a tenth of a second
+    pool = pv.PagePool([s["kc"]], [s["vc"]])
+    src, dst = pool.resize(table, lens, ref, new, stream=side)
+    side.synchronize()
+    assert lens.tolist() == [20, 3, 0, 33] and ref.tolist() == [1] * 6 + [0] * 6 and src.tolist() == [-1] * n == dst.tolist()
+    torch.cuda.synchronize()
+    assert pool.device_errors() == 0
