@@ -417,7 +417,8 @@ int pa_pages_fork(const pa_pages_desc* desc, int32_t* block_table, int32_t* cont
  * too (the caller copies copy_src[b] to copy_dst[b] with pa_pages_copy before
  * it writes; -1, -1 where there is none), then its new pages. When all holders of
  * such a page grow in the call, the last of them keeps it. A growing row whose
- * partly filled last page has count 0 is left as it was (REFS). The first growing row that
+ * partly filled last page has count 0, or a count of 2 or more that as many
+ * growing rows before it have used up, is left as it was (REFS). The first growing row that
  * the free pages do not cover and every growing row behind it are left as they
  * were (NO_PAGES).
  *   copy_src, copy_dst  [num_seqs] int32, out

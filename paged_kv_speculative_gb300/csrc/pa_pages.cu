@@ -181,6 +181,10 @@ __global__ void __launch_bounds__(kThreads) pages_resize_kernel(PagesDesc d, int
       int rank = 0;  // growing rows before this one with the same shared page
       for (int j = 0; j < b; ++j) rank += tails[j] == tail;
       copy = rank != held - 1;  // every holder grows and this is the last: it keeps the page
+      if (rank >= held) {       // more holders than the count knows: taking it down further would free a page that one of them keeps
+        flag(err, kErrRefs);
+        grows = copy = false;
+      }
     }
   }
   // a row cannot get more pages than there are: the sum stays in range

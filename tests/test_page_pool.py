@@ -409,3 +409,20 @@ def test_pool_arguments_are_checked():
         pool.fork(table, lens, ref, i32([0, 0]), i32([0]))
     with pytest.raises(ValueError):
         pool.copy(i32([0]), i32([0, 1]))
+
+
+@pytest.mark.gpu
+def test_more_growing_rows_than_a_page_counts():
+    """Three rows hold a page that counts two: the first copies it, the second keeps it, the third is refused; no page that a row
+    holds counts as free."""
+    m = Model(5, 4, 10)
+    m.resize([20, 0, 0, 0, 7])
+    m.fork([0, 0], [1, 2])
+    d = Device(m)
+    d.ref[1] = 2
+    src, dst = d.pool.resize(*d.args(), i32([25, 40, 40, -1, 9]))
+    assert d.pool.device_errors() == pv.DEVERR_REFS
+    assert d.lens.tolist() == [25, 40, 20, 0, 9]
+    assert (src.tolist(), dst.tolist()) == ([1, -1, -1, -1, -1], [3, -1, -1, -1, -1])
+    assert d.ref.tolist() == [3, 1, 1, 1, 1, 0, 0, 0, 0, 0]
+    assert d.table[:3, :3].tolist() == [[0, 3, -1], [0, 1, 4], [0, 1, -1]]
