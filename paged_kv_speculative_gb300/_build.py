@@ -2,10 +2,11 @@
 
 Each translation unit is compiled by its own nvcc process (in parallel) and
 then linked into one shared library with the CUDA runtime linked statically,
-so loading it needs no CUDA toolkit on the library path. Beside it, ``_lib/pa_fast.so``
+so loading it needs no CUDA toolkit on the library path. Beside it, ``_lib/pa_fast-*``
 is the binding's short way into the prompt-side calls (host code over torch's
 headers); the binding works without it, each of those calls taking some ten
-microseconds longer on the host.
+microseconds longer on the host. It is made for one torch and one Python, which
+its name says: another one does not load it.
 """
 from __future__ import annotations
 
@@ -21,7 +22,6 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "libpa_verify.so")
-FAST = os.path.join(LIBDIR, "pa_fast.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["pa_capi.cpp", "pa_split_bf16.cu", "pa_split_fp8.cu", "pa_combine.cu", "pa_kv_write.cu", "pa_verdict.cu", "pa_tc_split.cu", "pa_tc_split_d256.cu", "pa_tc_split_d64.cu", "pa_static.cu", "pa_dyn_plan.cu",
            "pa_prefill_capi.cpp", "pa_pages.cu", "pa_rope.cu", "pa_chunk.cu"]
@@ -33,6 +33,19 @@ def nvcc() -> str:
     if not os.path.exists(cand):
         raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libpa_verify.so")
     return cand
+
+
+def fast_path() -> str:
+    """Where pa_fast stands for the torch and the Python that run; "" without torch."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return os.path.join(LIBDIR, f"pa_fast-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _current(path: str) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
 
 
 def _deps_mtime() -> float:
@@ -53,37 +66,46 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_fast() -> None:
+_fast_failed = False  # tried once a process
+
+
+def _compile_fast(fast: str) -> None:
     """Compiles pa_fast.cpp against the installed torch; says so and goes on when that cannot be done."""
+    global _fast_failed
     try:
         import torch
         root = os.path.dirname(torch.__file__)
         cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
         inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], cuda]
-        tmp = FAST + f".tmp{os.getpid()}"
+        tmp = fast + f".tmp{os.getpid()}"
         subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                         *[f"-I{i}" for i in inc], os.path.join(CSRC, "pa_fast.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
                         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], check=True)
-        os.replace(tmp, FAST)
+        os.replace(tmp, fast)
     except Exception as e:  # the binding's Python code does the same work
-        if os.path.exists(FAST):
-            os.remove(FAST)
-        print(f"pa_fast.so was not built ({e}): calls take longer on the host", file=sys.stderr)
+        _fast_failed = True
+        if os.path.exists(fast):
+            os.remove(fast)
+        print(f"pa_fast was not built ({e}): calls take longer on the host", file=sys.stderr)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the library if any source is newer than it; returns its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    """Compiles the library, and pa_fast, if a source is newer or they are not there; returns the library's path."""
+    fast = fast_path()
+    want_lib, want_fast = force or not _current(LIB), bool(fast) and not _fast_failed and (force or not _current(fast))
+    if not want_lib and not want_fast:
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        fast = ex.submit(_compile_fast)
-        objs = list(ex.map(_compile, SOURCES))
-        fast.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs], check=True)
-    os.replace(tmp, LIB)
+        made = ex.submit(_compile_fast, fast) if want_fast else None
+        objs = list(ex.map(_compile, SOURCES)) if want_lib else []
+        if made:
+            made.result()
+    if want_lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs], check=True)
+        os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -430,12 +430,13 @@ def _fast():
     global _fast_module
     if _fast_module is None:
         _fast_module = False
-        if os.path.exists(_build.FAST):
-            spec = importlib.util.spec_from_file_location("pa_fast", _build.FAST)
+        path = _build.fast_path()
+        if os.path.exists(path):
+            spec = importlib.util.spec_from_file_location("pa_fast", path)
             m = importlib.util.module_from_spec(spec)
             try:
                 spec.loader.exec_module(m)
-            except ImportError:  # built against another torch
+            except ImportError:  # something it links is not there
                 return False
             L = lib()
             m.init(*[ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -1,5 +1,7 @@
 """The prompt-side calls of the binding, which has two ways into the C ABI: the module pa_fast and Python."""
 import math
+import os
+import sysconfig
 
 import pytest
 import torch
@@ -126,3 +128,17 @@ def test_a_new_object_on_another_stream(way):
     assert lens.tolist() == [20, 3, 0, 33] and ref.tolist() == [1] * 6 + [0] * 6 and src.tolist() == [-1] * n == dst.tolist()
     torch.cuda.synchronize()
     assert pool.device_errors() == 0
+
+
+# ------------------------------------------------------------------ the module
+def test_the_module_is_made_for_one_torch_and_apart_from_the_library(monkeypatch, tmp_path):
+    path, lib = _build.fast_path(), os.path.getmtime(_build.LIB)
+    assert os.path.exists(path) and path.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(_build, "LIBDIR", str(tmp_path))
+    assert not os.path.exists(_build.fast_path())
+    _build.build()
+    assert os.path.exists(_build.fast_path()) and os.path.getmtime(_build.LIB) == lib
+    monkeypatch.setattr(torch, "__version__", "0.0")  # the module of another torch is not looked at
+    assert _build.fast_path() != path and not os.path.exists(_build.fast_path())
+    monkeypatch.setattr(pv, "_fast_module", None)
+    assert pv._fast() is False
