@@ -10,6 +10,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <memory>
@@ -78,15 +79,12 @@ pa_stream_t stream_of(int dev) { return reinterpret_cast<pa_stream_t>(c10::cuda:
 bool current(int dev) { return c10::cuda::current_device() == dev; }
 at::Tensor ints(at::IntArrayRef shape, const at::Tensor& like) { return at::empty(shape, like.options().dtype(at::kInt)); }
 
-// body() returns a new reference; C++ exceptions become Python ones
+// body() returns a new reference; C++ exceptions become the Python ones that torch makes of them (OutOfMemoryError, ...)
 template <typename F>
 PyObject* guarded(F body) {
-  try {
-    return body();
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return body();
+  END_HANDLE_TH_ERRORS
 }
 PyObject* none() { Py_RETURN_NONE; }
 

@@ -142,3 +142,25 @@ def test_the_module_is_made_for_one_torch_and_apart_from_the_library(monkeypatch
     assert _build.fast_path() != path and not os.path.exists(_build.fast_path())
     monkeypatch.setattr(pv, "_fast_module", None)
     assert pv._fast() is False
+
+
+@pytest.mark.gpu
+def test_out_of_memory_is_torchs_error(way):
+    """Outputs of their own, with no memory for them."""
+    t, i32 = 1 << 18, dict(dtype=torch.int32, device="cuda")
+    s = setup(pv.KV_BF16)
+    s["q"] = torch.zeros((t, 4, 128), dtype=torch.bfloat16, device="cuda")  # 256 MB
+    s["k"] = s["v"] = torch.zeros((t, 2, 128), dtype=torch.bfloat16, device="cuda")
+    s["positions"], s["slots"] = torch.zeros((2, t), **i32), torch.full((t,), -1, dtype=torch.int64, device="cuda")
+    call = pv.ChunkAttention(4, 2, 128, pv.KV_BF16, 12, 4, max_seqs=2)
+    rope(s)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 24)) / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            rope(s)
+        with pytest.raises(torch.OutOfMemoryError):
+            call(*[s[n] for n in CHUNK], 1 / math.sqrt(128))
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    rope(s)
