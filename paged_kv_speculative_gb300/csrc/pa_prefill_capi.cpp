@@ -283,7 +283,7 @@ int pa_chunk_attention(const pa_chunk_desc* desc, const void* q, const void* k_c
   p.ql = query_lens;
   p.out = static_cast<uint16_t*>(out);
   p.ws = static_cast<uint8_t*>(workspace);
-  p.q_stride = d.q_stride ? d.q_stride : static_cast<int64_t>(d.num_q_heads) * d.head_dim;
+  p.q_stride = d.q_stride && d.num_tokens > 1 ? d.q_stride : static_cast<int64_t>(d.num_q_heads) * d.head_dim;  // one row has none
   p.scale = softmax_scale;
   p.num_seqs = d.num_seqs;
   p.num_tokens = d.num_tokens;
