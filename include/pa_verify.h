@@ -570,7 +570,7 @@ typedef struct {
   int64_t q_stride;
 } pa_chunk_desc;
 
-/* Depends on num_q_heads, num_kv_heads, head_dim, kv_dtype and sm_count; 0 for a desc that is refused. */
+/* Depends on head_dim and the number of SMs alone; 0 for a desc that is refused. */
 size_t pa_chunk_workspace_bytes(const pa_chunk_desc* desc);
 int pa_chunk_attention(const pa_chunk_desc* desc, const void* q, const void* k_cache, const void* v_cache,
                        const float* k_scale, const float* v_scale, const int32_t* block_table,

@@ -431,9 +431,11 @@ __global__ void __launch_bounds__(ChunkCfg<FP8, D>::kThreads, 1)
     *abort_flag = 0;
     *progress = 0;
     fence_mbar_init();
-    prefetch_tmap(&tmk);
-    prefetch_tmap(&tmv);
-    prefetch_tmap(&tmq);
+    if constexpr (!FP8) {
+      prefetch_tmap(&tmk);
+      prefetch_tmap(&tmv);
+      prefetch_tmap(&tmq);
+    }
   }
   chained_wait();
   __syncwarp();

@@ -99,7 +99,7 @@ struct ChunkParams {
   int32_t num_seqs, num_tokens, num_q_heads, num_kv_heads, num_pages, bt_stride, sms;
   int32_t group, tq;  // q heads of a KV head; tokens of a 128-row tile, floor(128 / group)
 };
-size_t chunk_workspace_bytes(int head_dim, int fp8, int num_q_heads, int num_kv_heads, int sms);
+size_t chunk_workspace_bytes(int head_dim, int sms);
 cudaError_t launch_chunk(int head_dim, int fp8, const ChunkParams& p, cudaStream_t stream);
 
 }  // namespace pav

@@ -245,7 +245,7 @@ size_t pa_chunk_workspace_bytes(const pa_chunk_desc* desc) {
   ok();
   int sms = 0;
   if (check_chunk_desc(desc, &sms)) return 0;
-  return chunk_workspace_bytes(desc->head_dim, desc->kv_dtype == PA_KV_FP8_E4M3, desc->num_q_heads, desc->num_kv_heads, sms);
+  return chunk_workspace_bytes(desc->head_dim, sms);
 }
 
 int pa_chunk_attention(const pa_chunk_desc* desc, const void* q, const void* k_cache, const void* v_cache,
@@ -269,9 +269,7 @@ int pa_chunk_attention(const pa_chunk_desc* desc, const void* q, const void* k_c
     return report_error(PA_ERR_INVALID, "int32 arrays must be 4-byte aligned");
   if (!(std::isfinite(softmax_scale) && softmax_scale > 0.f))
     return report_error(PA_ERR_INVALID, "softmax_scale must be finite and > 0");
-  if (int rc = check_workspace(workspace, workspace_bytes,
-                               chunk_workspace_bytes(d.head_dim, fp8 ? 1 : 0, d.num_q_heads, d.num_kv_heads, sms)))
-    return rc;
+  if (int rc = check_workspace(workspace, workspace_bytes, chunk_workspace_bytes(d.head_dim, sms))) return rc;
   ChunkParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.k_cache = k_cache;
