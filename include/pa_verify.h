@@ -547,8 +547,9 @@ int pa_rope_write(const pa_rope_desc* desc, const void* q, const void* k, const 
  * valid key may reach up to 256 / group tokens of its sequence before that key,
  * which do not see it (0 x NaN in a product of tiles); K has no such effect.
  * FP8: a key counts as code x scale rounded to 11 bits, in steps of 2^-27 of the
- * largest scale among its tile's keys where that is coarser; a value as code x
- * scale rounded to bf16. Softmax weights are bf16 for both cache types. Scales
+ * largest scale among its tile's keys where that is coarser; a query entry in
+ * steps of 2^-24 of the power of two at or below its row's largest (so it keeps
+ * its bits down to 2^-17 of that); a value as code x scale rounded to bf16. Softmax weights are bf16 for both cache types. Scales
  * are finite and <= 1e30; V scales below 2^-87 lose bits of the smallest codes.
  * A batch of query lengths up to 8 with FP8 KV is faster with pa_verify_run (about
  * twice at head_dim 128); bf16 takes the same time in both.

@@ -27,7 +27,8 @@
 // they wait for their next scores: one page of K or V a warp and tile, read from global memory (which warp 0, a few tiles
 // ahead, brings into L2), codes times scale, written in the layout of the bf16 tiles; everything behind is the bf16 path. K and Q are
 // f16: 11 bits (a key's entry is off by 2^-11 of itself at most, where E4M3 left 2^-4), so a K tile is scaled by 2^(4 - e), 2^e just
-// above its largest scale, which its scores are multiplied back by, and a row of Q by a power of two.
+// above its largest scale, which its scores are multiplied back by, and a row of Q by the power of two that puts its largest entry in
+// [1, 2): bf16's 8 bits then stay down to 2^-17 of that power, below it entries count in steps of 2^-24.
 // P and V are bf16, as there: P has to reach as far down as l does. In f16 a weight below 2^-25 of the reference is 0, and behind one
 // key that stands 17.4 nats above the others their whole part of the output goes (the cost: single tokens 159.5 to 167 us,
 // 512 tokens over 16384, 8/1 heads of 256, 110 to 114, 1024 over 8192 170.5 either way). V counts in 2^30, so that scales of
