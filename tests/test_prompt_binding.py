@@ -157,6 +157,10 @@ def test_out_of_memory_is_torchs_error(way):
     torch.cuda.empty_cache()
     torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 24)) / torch.cuda.get_device_properties(0).total_memory)
     try:
+        held = []  # what other tests left free, in pieces that an output does not fit into
+        with pytest.raises(torch.OutOfMemoryError):
+            while True:
+                held.append(torch.empty(1 << 26, dtype=torch.uint8, device="cuda"))
         with pytest.raises(torch.OutOfMemoryError):
             rope(s)
         with pytest.raises(torch.OutOfMemoryError):
