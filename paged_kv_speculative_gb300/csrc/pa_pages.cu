@@ -488,7 +488,7 @@ cudaError_t launch_pages_fork(const PagesDesc& d, int32_t* table, int32_t* lens,
 cudaError_t launch_pages_resize(const PagesDesc& d, int32_t* table, int32_t* lens, int32_t* ref, const int32_t* new_lens,
                                 int32_t* copy_src, int32_t* copy_dst, uint32_t* err, void* ws, cudaStream_t stream) {
   const bool small = static_cast<int64_t>(d.num_seqs) * d.stride <= 16384;
-  const int grid = small ? 1 : d.num_seqs < 304 ? d.num_seqs : 304;
+  const int grid = small ? 1 : d.num_seqs < 304 ? d.num_seqs : 304;  // at most two blocks for each of GB300's 152 SMs
   return launch_chained(pages_resize_kernel, grid, kThreads, 0, stream, d, table, lens, ref, new_lens, copy_src, copy_dst, err,
                                                      static_cast<uint32_t*>(ws), static_cast<int32_t*>(ws) + kTicketInts);
 }

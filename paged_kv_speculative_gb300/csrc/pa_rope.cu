@@ -60,8 +60,8 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
   }
 }
 
-// Eight warps a block, four groups an item, two blocks an SM (152 SMs): 8192 tokens of 32/4 heads of 128 (168 MB) in 35.6 us, where a
-// plain copy of as many bytes takes 32.8; 2 groups an item 41.0, 3 37.8; three blocks an SM with 2 groups 49.3.
+// Eight warps a block, four groups an item, two blocks an SM (GB300's 152): 8192 tokens of 32/4 heads of 128 (168 MB) in 32.5 us, where a
+// plain copy of as many bytes takes 32.8. When it took 35.6: 2 groups an item 41.0, 3 37.8; three blocks an SM with 2 groups 49.3.
 constexpr int kRopeWarps = 8;
 constexpr int kRopeBatch = 4;
 constexpr int kRopeGrid = 2 * 152;
@@ -216,8 +216,13 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 
 template <int D, bool FP8>
 cudaError_t launch_any(const RopeParams& p, cudaStream_t stream) {
-  // a few tokens: a warp for each group, so that they spread over the SMs; many: fewer angles per entry
-  return p.num_tokens < 512 ? launch<D, FP8, 1>(p, stream) : launch<D, FP8, kRopeBatch>(p, stream);
+  // While each group of heads of each token can have a warp of its own, it has: they spread over the SMs. Beyond, four share a token's
+  // angles and have their loads in flight at once. us, one and four groups an item, bf16, 128: 32/4 heads, 64 tokens (640 groups) 2.95
+  // and 3.19, 192 (1920) 3.34 and 3.56, 256 (2560) 4.20 and 3.75, 1024 8.6 and 6.1; 8/2 heads, 768 (2304) 3.44 and 3.63, 1024 (3072)
+  // 4.4 and 3.7; 64/8 heads, 128 (2560) 4.2 and 3.8; heads of 256, FP8, 192 (1920) 4.35 and 4.88, 256 (2560) 5.3 and 5.0.
+  constexpr int kHeads = 32 / (D / 16);
+  const int64_t groups = (p.num_q_heads + 2 * p.num_kv_heads + kHeads - 1) / kHeads;
+  return p.num_tokens * groups <= kRopeGrid * kRopeWarps ? launch<D, FP8, 1>(p, stream) : launch<D, FP8, kRopeBatch>(p, stream);
 }
 
 }  // namespace
