@@ -168,3 +168,101 @@ def test_out_of_memory_is_torchs_error(way):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     rope(s)
+
+
+# ------------------------------------------------------------------ both ways do the same
+def tables(s):
+    return s["table"].clone(), s["ctx"].clone(), s["ref"].clone()
+
+
+def everything(s):
+    """Every call once; what they return and leave, as host values."""
+    out, err = [], torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in s.items()}
+    out += [rope(s), rope(s, q_out=s["q"].clone(), pairs=pv.ROPE_NEIGHBOURS, error_flags=err), err, s["kc"], s["vc"], s["ks"], s["vs"]]
+    out += [chunk(s), chunk(s, out=torch.zeros_like(s["q"]))]
+    pool = pv.PagePool([s["kc"]], [s["vc"]], None if s["ks"] is None else [s["ks"]], None if s["vs"] is None else [s["vs"]])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table, lens, ref = tables(s)
+    out += [*pool.resize(table, lens, ref, i32([50, 0])), table.clone(), lens.clone(), ref.clone()]
+    pool.fork(table, lens, ref, i32([0]), i32([1]))
+    src, dst = pool.resize(table, lens, ref, i32([51, 53]))
+    pool.copy(src, dst)
+    out += [src, dst, table.clone(), lens.clone(), ref.clone(), s["kc"].clone(), s["vc"].clone()]
+    pool.resize(table, lens, ref, i32([0, -1]))
+    new = pool.compact(table, lens, ref)
+    out += [*new, table.clone(), ref.clone()]
+    in_place = pool.compact(table, lens, ref, in_place=True)
+    assert in_place[0] is table and in_place[1] is ref
+    pool.copy(in_place[2], in_place[3], in_place[4])
+    out += [*in_place, s["kc"], s["vc"], s["ks"], s["vs"]]
+    assert pool.device_errors() == 0
+    return [None if t is None else t.view(torch.uint8).cpu() if t.dtype in (torch.bfloat16, torch.float8_e4m3fn) else t.cpu() for t in out]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [pv.KV_BF16, pv.KV_FP8_E4M3])
+def test_both_ways_give_the_same(kv, monkeypatch):
+    s = setup(kv, seed=3)
+    assert pv._fast()
+    native = everything(s)
+    monkeypatch.setattr(pv, "_fast_module", False)
+    python = everything(s)
+    assert len(native) == len(python)
+    for i, (a, b) in enumerate(zip(native, python)):
+        assert (a is None and b is None) or torch.equal(a, b), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [pv.KV_BF16, pv.KV_FP8_E4M3])
+def test_both_ways_refuse_the_same(way, kv):
+    s = setup(kv)
+    fp8 = kv == pv.KV_FP8_E4M3
+
+    def refused(call, name, bad, error=ValueError):
+        with pytest.raises(error):
+            call({**s, name: bad})
+    for name, bad in (("q", s["q"].float()), ("q", s["q"].cpu()), ("q", s["q"][0]), ("k", s["k"][:3]), ("k", s["k"][:, :, :64]), ("v", s["v"].transpose(0, 1)),
+                      ("v", s["v"][:, :1]), ("positions", s["positions"].long()), ("positions", s["positions"][:, :2].contiguous()),
+                      ("positions", s["positions"].cpu()), ("positions", s["positions"][0]), ("inv_freq", s["inv_freq"].float()),
+                      ("pair_axis", s["pair_axis"][:5].contiguous()), ("pair_axis", s["pair_axis"].repeat(2)[::2]), ("slots", s["slots"].int()),
+                      ("slots", s["slots"][1:]), ("kc", s["kc"][:, :, :8]), ("vc", s["vc"][:3].contiguous()), ("vc", s["vc"].cpu())):
+        refused(rope, name, bad)
+    for name, bad in (("q", s["q"][:, :2]), ("q", s["q"].half()), ("kc", s["kc"][1:]), ("vc", s["vc"].transpose(1, 2)), ("table", s["table"].long()),
+                      ("table", s["table"][:, :3].contiguous()), ("table", s["table"][:1]), ("ctx", s["ctx"].long()), ("ctx", s["ctx"].cpu()),
+                      ("ql", s["ql"][:1]), ("ql", s["ql"].repeat(2)[::2])):
+        refused(chunk, name, bad)
+    if fp8:
+        for call in (rope, chunk):
+            for name in ("ks", "vs"):
+                for bad in (None, s[name].double(), s[name][1:], s[name].cpu()):
+                    refused(call, name, bad)
+    for kw in (dict(q_out=s["q"].float()), dict(q_out=s["q"][:3]), dict(q_out=s["q"].cpu()), dict(error_flags=torch.zeros(1, dtype=torch.int64, device="cuda")),
+               dict(error_flags=torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            rope(s, **kw)
+    for bad in (s["q"][:3], s["q"].float(), s["q"].cpu(), s["q"].repeat(1, 1, 2)[..., :128]):
+        with pytest.raises(ValueError):
+            chunk(s, out=bad)
+    with pytest.raises(pv.PaVerifyError):
+        rope(s, pairs=2)
+    with pytest.raises(pv.PaVerifyError):
+        pv.ChunkAttention(4, 2, 128, kv, 12, 4, max_seqs=2)(*[s[n] for n in CHUNK], -1.0)
+    pool = pv.PagePool([s["kc"]], [s["vc"]], [s["ks"]] if fp8 else None, [s["vs"]] if fp8 else None)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    table, lens, ref = tables(s)
+    for bad in ((table.long(), lens, ref), (table, lens.long(), ref), (table, lens, ref[:3]), (table, lens[:1], ref), (table.cpu(), lens, ref),
+                (table[:, ::2], lens, ref), (table[0], lens, ref)):
+        for call in (lambda *t: pool.resize(*t, i32([-1, -1])), lambda *t: pool.fork(*t, i32([0]), i32([1])), pool.compact):
+            with pytest.raises(ValueError):
+                call(*bad)
+    for call in (lambda: pool.resize(table, lens, ref, i32([1])), lambda: pool.resize(table, lens, ref, i32([1, 1]).long()),
+                 lambda: pool.fork(table, lens, ref, i32([0, 0]), i32([0])), lambda: pool.fork(table, lens, ref, i32([0]).cpu(), i32([0])),
+                 lambda: pool.copy(i32([0]), i32([0, 1])), lambda: pool.copy(i32([0]).long(), i32([1])), lambda: pool.copy(i32([[0]]), i32([[1]])),
+                 lambda: pool.copy(i32([0]), i32([1]), i32([1, 1])), lambda: pool.copy(i32([0]), i32([1]), i32([1]).cpu())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(pv.PaVerifyError):
+        pool.fork(table, lens, ref, i32([0] * 1025), i32([1] * 1025))
+    for a, b in zip((table, lens, ref), tables(s)):
+        assert torch.equal(a, b)
