@@ -266,3 +266,67 @@ def test_both_ways_refuse_the_same(way, kv):
         pool.fork(table, lens, ref, i32([0] * 1025), i32([1] * 1025))
     for a, b in zip((table, lens, ref), tables(s)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [pv.KV_BF16, pv.KV_FP8_E4M3])
+def test_a_whole_step_in_a_graph_beside_another_stream(way, kv):
+    """Resize, copy, rotary write and attention captured with torch's kernels between them and a second attention (its own workspace)
+    on a stream that forks off and joins; two graphs share the workspaces. Replays do what the calls do."""
+    pages, stride, t = 60, 10, 48
+    s = setup(kv, pages=pages, seed=9)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(10)
+    qkv = torch.randn((t, 8, 128), device="cuda", generator=g).to(torch.bfloat16)
+    pool = pv.PagePool([s["kc"]], [s["vc"]], None if s["ks"] is None else [s["ks"]], None if s["vs"] is None else [s["vs"]])
+    attend = [pv.ChunkAttention(4, 2, 128, kv, pages, stride, max_seqs=3) for _ in range(2)]
+    start = dict(table=i32([[-1] * stride] * 3), lens=i32([0] * 3), ref=i32([0] * pages))
+    now = {k: v.clone() for k, v in start.items()}
+    new, ql = i32([0] * 3), i32([0] * 3)
+    positions = torch.arange(t, **dict(dtype=torch.int32, device="cuda")).repeat(2, 1)
+    slots = torch.zeros(t, dtype=torch.int64, device="cuda")
+    caches = (s["kc"], s["vc"], s["ks"], s["vs"])
+    side = torch.cuda.Stream()
+
+    def step():
+        args = now["table"], now["lens"], now["ref"]
+        src, dst = pool.resize(*args, new)
+        pool.copy(src, dst)
+        row = torch.repeat_interleave(torch.arange(3, device="cuda"), ql.long(), output_size=t)
+        first = (ql.cumsum(0) - ql).long()
+        at = now["lens"][row].long() - ql[row].long() + torch.arange(t, device="cuda") - first[row]
+        slots.copy_(now["table"][row, at // PAGE].long() * PAGE + at % PAGE)
+        q = pv.rope_write(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], positions, s["inv_freq"], s["pair_axis"], slots, *caches, kv)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b = attend[1](qkv[:, 2:6], *caches, now["table"], now["lens"], ql, 0.1)
+        a = attend[0](q, *caches, now["table"], now["lens"], ql, 0.09)
+        main.wait_stream(side)
+        return a, b, q, src, dst
+
+    def run(lens, count, how):
+        new.copy_(i32(lens))
+        ql.copy_(i32(count))
+        out = how()
+        torch.cuda.synchronize()
+        return [x.clone() for x in (*out, *now.values())]
+
+    plan = [([40, 8, -1], [40, 8, 0]), ([56, 24, 16], [16, 16, 16]), ([57, 0, 63], [1, 0, 47]), ([105, -1, -1], [48, 0, 0])]
+    want = [run(*p, step) for p in plan]
+    begin = [c.clone() for c in caches if c is not None]
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(step())
+    for k, v in start.items():
+        now[k].copy_(v)
+    for i, (p, w) in enumerate(zip(plan, want)):
+        def replay():
+            graphs[i % 2].replay()
+            return outs[i % 2]
+        for j, (x, y) in enumerate(zip(run(*p, replay), w)):
+            assert torch.equal(x, y), (i, j)
+    for c, b in zip([c for c in caches if c is not None], begin):
+        assert torch.equal(c.view(torch.uint8), b.view(torch.uint8))
+    assert pool.device_errors() == 0 and attend[0].device_errors() == 0 == attend[1].device_errors()
