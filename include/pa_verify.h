@@ -494,8 +494,9 @@ int pa_pages_copy(const pa_pool_desc* desc, const int32_t* copy_src, const int32
  *                q_out. No two tokens share a slot.
  *   q_out        [num_tokens, Hq, D] bf16, q_out_stride; may be q itself (same
  *                stride), else it must not overlap the inputs
- *   caches, scales, error_flags as in pa_kv_write (caches 16-byte aligned).
- *                FP8: quantised from the fp32 rotated values, s = amax / 448 (1
+ *   caches, scales, error_flags as in pa_kv_write (caches 16-byte aligned; FP8
+ *                rows of head_dim 64 are stored, but no attention here reads
+ *                them). FP8: quantised from the fp32 rotated values, s = amax / 448 (1
  *                when amax = 0), code = E4M3(x / s).
  * q, k, v, q_out 16-byte aligned. rot_dim a multiple of 16, 0 .. D; num_axes
  * 1 .. 4. Asynchronous on `stream`; allocates nothing.
@@ -551,8 +552,13 @@ int pa_rope_write(const pa_rope_desc* desc, const void* q, const void* k, const 
  * steps of 2^-24 of the power of two at or below its row's largest (so it keeps
  * its bits down to 2^-17 of that); a value as code x scale rounded to bf16. Softmax weights are bf16 for both cache types. Scales
  * are finite and <= 1e30; V scales below 2^-87 lose bits of the smallest codes.
- * A batch of query lengths up to 8 with FP8 KV is faster with pa_verify_run (about
- * twice at head_dim 128); bf16 takes the same time in both.
+ * Weights and outputs are summed in fp32 on the tensor cores, whose additions round
+ * towards zero: where one CTA walks n keys of like weights for its rows (all of a
+ * context, for prompts; a share of it, for few rows), an output loses about n 2^-28
+ * of itself: 0.5 % at n = 2^20, 4 % at 2^23.
+ * A batch of query lengths up to 8 with FP8 KV is faster with pa_verify_run (1.4 to
+ * 2.3 times for 32 sequences of 8192), one with bf16 KV by 2 to 13 % at head_dim 128
+ * and slower by 12 to 18 % at 256.
  * head_dim 64, 128 or 256 (bf16 KV), 128 or 256 (FP8 KV); group Hq / Hkv up to
  * 128; num_seqs 0 .. 1024. Asynchronous on `stream`; allocates nothing. Two calls that
  * share a workspace must not overlap on the GPU.

@@ -33,12 +33,13 @@
 // key that stands 17.4 nats above the others their whole part of the output goes (the cost: single tokens 159.5 to 167 us,
 // 512 tokens over 16384, 8/1 heads of 256, 110 to 114, 1024 over 8192 170.5 either way). V counts in 2^30, so that scales of
 // up to 1e30 sum in fp32 and those down to 2^-87 keep every code.
-// Measured for 1024 tokens over 8192, 32/4 heads of 128: in 8 bits throughout with P in two E4M3 terms 297 us (scales at every
-// score are 160 16-byte shared loads a warp and tile); with V alone widened by two warps of their own 204 us; with six warps of
-// their own for both 181 to 185, and 113 to 123 for 512 tokens over 16384, 8/1 heads of 256; this way 177 and 114. bf16: 121.
-// Single tokens, 32 sequences of 8192 keys: bf16 118 us (537 MB; the verify kernel 110), 8 bits 169 (the verify kernel 84: it
-// widens nothing). The second softmax group taking every other key tile of such units: 109 and 175, and prompts lost 10 % to
-// the registers that it took; not done.
+// Measured, us, calls back to back: 1024 tokens over 8192, 32/4 heads of 128: bf16 115, 8 bits 170.5; 512 over 16384, 8/1 heads of 256, 8
+// bits 114; 1024 over 8192, 32/4 heads of 64: 101.5. Single tokens, 32 sequences of 8192 keys: bf16 107.6 (537 MB; the verify kernel
+// 95), 8 bits 167 (the verify kernel 75: it widens nothing). With L2 emptied before each call 121.5, 176, 119, 107, 118 and 172.
+// Tried for 8 bits and slower when the first of these took 177, L2 emptied: V alone widened, by two warps of their own, 204; six
+// warps of their own for both 181 to 185; the second softmax group taking every other key tile of single tokens 175 for 169 (and
+// prompts lost 10 % to the registers that it took). 8 bits throughout, P in two E4M3 terms, took 297 with one thread a row, when bf16
+// took 158: scales at every score are 160 16-byte shared loads a warp and tile.
 #pragma once
 
 #include "pa_device.cuh"
@@ -182,11 +183,12 @@ struct __align__(16) ChunkTile {
 };
 constexpr float kChunkVUnit = 1073741824.f;  // FP8: what V, and with it O, counts in (2^30)
 
-// Line length of a unit: its visible keys plus this many tokens for its start and end (three tiles; 32 ragged sequences 73.9 us,
-// with two or four 75.7; 64 prompts of 300 tokens 139 and 144).
+// Line length of a unit: its visible keys plus this many tokens for its start and end (three tiles; 32 ragged sequences 71.3 us,
+// with two 72.8, four 72.9; 64 prompts of 300 tokens 137.4, 142.9, 137.3).
 constexpr int kChunkUnitCost = 384;
-// A CTA gets at least this much of the line: below it, splitting costs more than it saves (two sequences of 1500 keys, 40 tokens
-// each: 20.6 us, with 384 22.7, 1024 33; four decode tokens over 3000 18.5, 18.5, 26.7; two short sequences, 512: 14.4 for 12.4).
+// A CTA gets at least this much of the line: below it, splitting costs more than it saves (us with 128, 256, 384, 512, 1024: two
+// sequences of 1500 keys, 40 tokens each, 22.7, 22.2, 22.9, 24.0, 29.4; four decode tokens over 3000 17.2, 17.2, 17.1, 18.0, 23.5; two
+// short sequences 10.3, 10.3, 10.2, 12.5, 12.5).
 constexpr int kChunkMinPiece = 256;
 
 struct ChunkPos {  // a place on the line: tile t of unit (b, g, j); b = num_seqs: the end
