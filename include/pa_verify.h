@@ -550,12 +550,13 @@ int pa_rope_write(const pa_rope_desc* desc, const void* q, const void* k, const 
  * FP8: a key counts as code x scale rounded to 11 bits, in steps of 2^-27 of the
  * largest scale among its tile's keys where that is coarser; a query entry in
  * steps of 2^-24 of the power of two at or below its row's largest (so it keeps
- * its bits down to 2^-17 of that); a value as code x scale rounded to bf16. Softmax weights are bf16 for both cache types. Scales
- * are finite and <= 1e30; V scales below 2^-87 lose bits of the smallest codes.
- * Weights and outputs are summed in fp32 on the tensor cores, whose additions round
- * towards zero: where one CTA walks n keys of like weights for its rows (all of a
- * context, for prompts; a share of it, for few rows), an output loses about n 2^-28
- * of itself: 0.5 % at n = 2^20, 4 % at 2^23.
+ * its bits down to 2^-17 of that); a value as code x scale rounded to bf16.
+ * Scales are finite and <= 1e30; V scales below 2^-87 lose bits of the smallest
+ * codes. Softmax weights are rounded to bf16 for both cache types.
+ * Outputs are summed in fp32 on the tensor cores, whose additions round towards
+ * zero: where one CTA walks n keys of like weights for its rows (all of a context,
+ * for prompts; a share of it, for few rows), an output loses about n 2^-28 of
+ * itself: 0.5 % at n = 2^20, 4 % at 2^23.
  * A batch of query lengths up to 8 with FP8 KV is faster with pa_verify_run (1.4 to
  * 2.3 times for 32 sequences of 8192), one with bf16 KV by 2 to 13 % at head_dim 128
  * and slower by 12 to 18 % at 256.
