@@ -218,7 +218,7 @@ template <int D, bool FP8>
 cudaError_t launch_any(const RopeParams& p, cudaStream_t stream) {
   // While each group of heads of each token can have a warp of its own, it has: they spread over the SMs. Beyond, four share a token's
   // angles and have their loads in flight at once. us, one and four groups an item, bf16, 128: 32/4 heads, 64 tokens (640 groups) 2.95
-  // and 3.19, 192 (1920) 3.34 and 3.56, 256 (2560) 4.20 and 3.75, 1024 8.6 and 6.1; 8/2 heads, 768 (2304) 3.44 and 3.63, 1024 (3072)
+  // and 3.19, 192 (1920) 3.34 and 3.56, 256 (2560) 4.20 and 3.75, 1024 8.6 and 6.1; 8/2 heads, 768 (2304) 3.44 and 3.63, 1024
   // 4.4 and 3.7; 64/8 heads, 128 (2560) 4.2 and 3.8; heads of 256, FP8, 192 (1920) 4.35 and 4.88, 256 (2560) 5.3 and 5.0.
   constexpr int kHeads = 32 / (D / 16);
   const int64_t groups = (p.num_q_heads + 2 * p.num_kv_heads + kHeads - 1) / kHeads;
